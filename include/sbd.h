@@ -256,6 +256,9 @@ delta_status delta_apply_checked(uint16_t *snapshot, int64_t n, const int32_t *i
  *  offsets             DEVICE int64[nparams+1] as delta_diff_many wrote it;
  *                      read on the GPU, so this call can follow delta_diff_many
  *                      on the same stream without a host round trip.
+ *                      offsets[0] is 0.  With another value nothing outside
+ *                      the buffers is read or written, and the entries in
+ *                      front of it count as parameter 0's.
  *  max_nnz             (host) capacity of idx/val: entries j < min(
  *                      offsets[nparams], max_nnz) are applied.  The caller must
  *                      not apply a truncated delta (check the total first).
@@ -699,7 +702,8 @@ delta_status mxfp4_dequantize_many(int32_t nparams, const uint8_t *const *code_p
  * touched one, and with a dense delta all).
  *  snap_ptrs           (host) the bf16 snapshots, updated in place; their
  *                      shapes in rows and cols.
- *  idx, val, offsets, max_nnz, violations  as delta_apply_many.  The order
+ *  idx, val, offsets, max_nnz, violations  as delta_apply_many (offsets[0]
+ *                      is 0, and another value is treated alike).  The order
  *                      precondition is that of delta_apply; where it is broken,
  *                      the blocks of the entries concerned are unspecified too.
  * Other arguments and errors as mxfp4_quantize_many; no snapshot may overlap

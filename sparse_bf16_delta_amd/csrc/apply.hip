@@ -396,7 +396,7 @@ __device__ __forceinline__ bool apply_chunk(
     }
     int32_t prev = 0;
     bool have_prev = false;
-    if (violations != nullptr && jt > seg_start) {
+    if (violations != nullptr && jt > seg_start && jt > 0) {
       prev = idx[jt - 1];
       have_prev = true;
     }
@@ -715,8 +715,9 @@ __device__ __forceinline__ bool apply_big_chunk(
     if (in_range && !interior) *global_ptr(d.snap + i) = vv;
     if (violations != nullptr) {
       int32_t prev = __shfl_up(iv, 1, 64);
-      if (lane == 0 && j > seg_start) prev = idx[j - 1];
-      bad = (!in_range || (j > seg_start && iv <= prev)) ? 1 : 0;
+      const bool have_prev = j > seg_start && j > 0;
+      if (lane == 0 && have_prev) prev = idx[j - 1];
+      bad = (!in_range || (have_prev && iv <= prev)) ? 1 : 0;
     }
   }
   if (mode == kSegments) {

@@ -257,7 +257,8 @@ __device__ __forceinline__ void apply_step(ApplyShared<kTile>& sh, const ApplySt
         group[k] = at.block / kGroupBlocks;
         elem[k] = uint32_t(at.block % kGroupBlocks) * kMxBlock + at.elem;
         first[k] = true;
-        if (j > st.offsets[p] && j > 0) {
+        // what lies in front of offsets[0] is parameter 0's
+        if (j > 0 && (j > st.offsets[p] || p == 0)) {
           const Spot last = spot_of(mine, st.idx[j - 1]);
           first[k] = last.block < 0 || last.block / kGroupBlocks != group[k];
         }
@@ -369,16 +370,12 @@ __global__ __launch_bounds__(kMxGroup) void mx_apply_kernel(
     const int32_t* __restrict__ idx, const uint16_t* __restrict__ val,
     const int64_t* __restrict__ offsets, int64_t max_nnz) {
   __shared__ ApplyShared<kTile> sh;
-  // no entry outside [0, max_nnz) is read, and a search starts only where its
-  // first step holds
+  // no entry outside [0, max_nnz) is read
   int64_t total = offsets[nparams];
   total = total < max_nnz ? total : max_nnz;
-  const int64_t begin = offsets[0] > 0 ? offsets[0] : 0;
-  for (int64_t base = int64_t(blockIdx.x) * kTile; base < total;
-       base += int64_t(gridDim.x) * kTile) {
-    const int64_t start = base > begin ? base : begin;
-    const int64_t end = base + kTile < total ? base + kTile : total;
-    if (start >= end) continue;  // the same in all lanes
+  for (int64_t start = int64_t(blockIdx.x) * kTile; start < total;
+       start += int64_t(gridDim.x) * kTile) {
+    const int64_t end = start + kTile < total ? start + kTile : total;
     ApplyStep st{idx, val, offsets, start, total, int(end - start), 0, 0};
     if (table) {
       if (threadIdx.x < 64) {

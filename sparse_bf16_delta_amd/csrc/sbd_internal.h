@@ -102,15 +102,18 @@ struct SnapParam {
 // Called by the 64 lanes of wave 0 only: the largest p in [0, nparams) with
 // offsets[p] <= j -- the non-empty parameter holding entry j of a
 // concatenated delta -- by a 64-way search (each step probes 64 evenly
-// spaced offsets at once; two steps for up to 4096 parameters).
+// spaced offsets at once; two steps for up to 4096 parameters).  An entry in
+// front of offsets[0] (which a well-formed delta does not have, and offsets
+// that came over a wire may) counts as parameter 0's: no probe holds for it.
 __device__ __forceinline__ int32_t find_param_wave0(const int64_t* __restrict__ offsets,
                                                     int32_t nparams, int64_t j) {
   const int lane = threadIdx.x & 63;
-  int32_t lo = 0, hi = nparams;  // offsets[lo] <= j holds throughout
+  int32_t lo = 0, hi = nparams;  // offsets[lo] <= j holds throughout, or lo is 0
   while (hi - lo > 1) {
     const int32_t step = (hi - lo + 63) / 64;
     const int32_t probe = lo + lane * step;
     const uint64_t ok = __ballot(probe < hi && offsets[probe] <= j);
+    if (ok == 0u) break;  // the same in all lanes
     lo += (63 - __builtin_clzll(ok)) * step;
     hi = lo + step < hi ? lo + step : hi;
   }

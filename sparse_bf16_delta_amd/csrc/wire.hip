@@ -62,7 +62,8 @@ __global__ __launch_bounds__(kScanThreads) void wire_offsets_kernel(
   if (tid == 0) pos_offsets[nparams] = s_carry;
 }
 
-// Encode writes a position only if all its bytes fit `positions_capacity`.
+// Encode writes a position only if all its bytes lie in [0,
+// positions_capacity) (an entry in front of offsets[0] has none there).
 // Decode reads one only if its bytes lie inside the block
 // (`positions_capacity` is then the block's size) and inside its parameter's
 // span [pos_offsets[p], pos_offsets[p+1]); otherwise it writes -1 (never a
@@ -127,7 +128,7 @@ __global__ __launch_bounds__(kWireBlock) void wire_code_kernel(
               ++bad;
             }
           } else {
-            if (at + w <= positions_capacity) {
+            if (at >= 0 && at + w <= positions_capacity) {
               const uint32_t v = static_cast<uint32_t>(idx[j]);
               *global_ptr(half) = static_cast<uint16_t>(v & 0xFFFFu);
               if (w == 4) *global_ptr(half + 1) = static_cast<uint16_t>(v >> 16);
