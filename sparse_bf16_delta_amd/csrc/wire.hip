@@ -96,7 +96,9 @@ __global__ __launch_bounds__(kWireBlock) void wire_code_kernel(
       int32_t p = s_p0;
       int64_t seg_end = offsets[p + 1];
       int w = widths[p];
-      int64_t base = pos_offsets[p] - offsets[p] * w;  // byte of entry j is base + j * w
+      // byte of entry j is base + j * w; unsigned, since decode's offsets are
+      // not trusted and may leave int64
+      uint64_t base = uint64_t(pos_offsets[p]) - uint64_t(offsets[p]) * uint64_t(w);
       int64_t span_lo = kDecode ? pos_offsets[p] : 0;
       int64_t span_end = kDecode ? pos_offsets[p + 1] : 0;
       int64_t bad = 0;
@@ -109,16 +111,17 @@ __global__ __launch_bounds__(kWireBlock) void wire_code_kernel(
               seg_end = offsets[++p + 1];
             } while (seg_end <= j);
             w = widths[p];
-            base = pos_offsets[p] - offsets[p] * w;
+            base = uint64_t(pos_offsets[p]) - uint64_t(offsets[p]) * uint64_t(w);
             if constexpr (kDecode) {
               span_lo = pos_offsets[p];
               span_end = pos_offsets[p + 1];
             }
           }
-          const int64_t at = base + j * w;
+          const int64_t at = int64_t(base + uint64_t(j) * uint64_t(w));
           auto half = reinterpret_cast<uint16_t*>(positions + at);
           if constexpr (kDecode) {
-            if (at >= span_lo && at >= 0 && at + w <= span_end && at + w <= positions_capacity &&
+            // inside the block first: behind it at + w may wrap
+            if (at >= 0 && at <= positions_capacity - w && at >= span_lo && at + w <= span_end &&
                 (at & 1) == 0) {
               uint32_t v = *global_ptr(half);
               if (w == 4) v |= uint32_t(*global_ptr(half + 1)) << 16;
@@ -128,7 +131,7 @@ __global__ __launch_bounds__(kWireBlock) void wire_code_kernel(
               ++bad;
             }
           } else {
-            if (at >= 0 && at + w <= positions_capacity) {
+            if (at >= 0 && at <= positions_capacity - w) {
               const uint32_t v = static_cast<uint32_t>(idx[j]);
               *global_ptr(half) = static_cast<uint16_t>(v & 0xFFFFu);
               if (w == 4) *global_ptr(half + 1) = static_cast<uint16_t>(v >> 16);

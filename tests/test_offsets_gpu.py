@@ -108,3 +108,21 @@ def test_decode_reports_what_has_no_place(name):
     blocked = sbd.wire_encode_blocked(idx, off, numels)
     # 16-bit places within the parameter's first block: nothing here is lost
     assert torch.equal(sbd.wire_decode_blocked(blocked, started_at(off, 7), numels), idx)
+
+
+@pytest.mark.parametrize("first", [-(1 << 62) + 1, -(1 << 61) + 1, -(1 << 63)])
+def test_decode_of_places_at_the_end_of_int64(first):
+    """An entry's byte from such an offset lies just below 2^63, where the
+    position's own bytes pass it."""
+    numels = [70000, 300]  # 4 bytes and 2 bytes a position
+    snaps = [torch.zeros(n, device="cuda", dtype=torch.bfloat16) for n in numels]
+    idx, _, off = delta(snaps, 0.1, 6)
+    pos, po = sbd.wire_encode(idx, off, numels)
+    blocked = sbd.wire_encode_blocked(idx, off, numels)
+    bad = started_at(off, first)
+    for sizes in (numels, numels[::-1]):  # the first parameter's width is 4, then 2
+        with pytest.raises(DeltaError, match="malformed"):
+            sbd.wire_decode(pos, po, bad, sizes)
+    # the blocked form takes nothing but the entries' order from offsets
+    with pytest.raises(DeltaError, match="malformed"):
+        sbd.wire_decode_blocked(blocked, bad, numels)
