@@ -228,6 +228,12 @@ def mxfp4_apply_many_(snaps: Sequence[torch.Tensor], quants: Sequence[Mxfp4], id
     return snaps, quants
 
 
+def _no_graph(t, what: str):
+    if isinstance(t, torch.Tensor) and t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{what} requires a gradient, and mxfp4_matmul has none: detach it, or "
+                         "call under torch.no_grad()")
+
+
 def mxfp4_matmul(x: torch.Tensor | Mxfp4, w: Mxfp4, out: torch.Tensor | None = None,
                  out_dtype: torch.dtype | None = None) -> torch.Tensor:
     """y = Q(x) Q(w)^T with both sides in MXFP4, accumulated in float32 and
@@ -235,13 +241,16 @@ def mxfp4_matmul(x: torch.Tensor | Mxfp4, w: Mxfp4, out: torch.Tensor | None = N
     float16 or float32 tensor [..., k], quantised in the call exactly as
     mxfp4_quantize does, or an Mxfp4 [..., k].  Returns [..., n] in out_dtype
     (default: x's type, bfloat16 for an Mxfp4), or writes `out`.  A sampler's
-    product: no gradient flows through it."""
+    product, without a gradient: an x (or out) that requires one is refused
+    where gradients are recorded; detach it, or call under torch.no_grad()."""
     if not isinstance(w, Mxfp4):
         raise TypeError(f"w: expected an Mxfp4, got {type(w).__name__}")
     if len(w.shape) != 2:
         raise ValueError(f"w: expected a replica of shape [n, k], got {w.shape}")
     n, k = w.shape
     given = isinstance(x, Mxfp4)
+    _no_graph(x, "x")
+    _no_graph(out, "out")
     if not given:
         _grad(x, "x")
         if x.dim() == 0:
