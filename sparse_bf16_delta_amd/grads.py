@@ -5,11 +5,13 @@ whose two snapshots diff_many compares).
   grad_norm(grads)                 -- the norm of all tensors together
   clip_grads_(grads, max_norm)     -- times min(1, max_norm / (norm + 1e-6))
   grad_total(grads)                -- what ranks holding shards add up first
-  ClipPlan(grads)                  -- the same for a fixed list, every step
+  ClipPlan(grads)                  -- the same, every step, for gradients that
+                                      stay in their tensors
 
 Gradients are bfloat16, float16 or float32, mixed freely, each contiguous and
 all on one device; the norm is a float32 scalar on that device, and nothing is
-read back unless asked.  Every call may be captured into a graph.
+read back unless asked.  No call records an autograd graph, and every call may
+be captured into a HIP graph.
 """
 from __future__ import annotations
 
@@ -185,7 +187,14 @@ class ClipPlan:
     results and the norm are allocated once, outside any capture.  The runs of one plan share them,
     so they must follow one another (on one stream, or ordered by events);
     what a run returns is the plan's own scalar, and the next run overwrites
-    it."""
+    it.
+
+    The plan is made for these tensors: it keeps them alive and works at their
+    addresses.  A step that makes new gradient tensors leaves it with the old
+    ones, and torch's zero_grad() does so unless it is called with
+    set_to_none=False (or the gradients live in buffers of the trainer's own).
+    Pass the step's gradients as `grads`: others than the plan's are refused, on
+    the host, before anything is enqueued."""
 
     def __init__(self, grads: Sequence[torch.Tensor],
                  outs: Sequence[torch.Tensor] | None = None, norm_type: float = 2.0):
@@ -193,6 +202,7 @@ class ClipPlan:
         self._list = _List(grads, outs)
         lst = self._list
         self.device, self.nparams = lst.device, lst.nparams
+        self._what = [(g.data_ptr(), g.numel(), g.dtype) for g in lst.grads]
         with torch.cuda.device(self.device):
             self.ws = lst.workspace()
             self._norm = torch.empty((), dtype=torch.float32, device=self.device)
@@ -201,18 +211,37 @@ class ClipPlan:
             # runs may come on any stream
             torch.cuda.current_stream(self.device).synchronize()
 
-    def norm(self) -> torch.Tensor:
+    def _same(self, grads):
+        """Refuses gradients that are not where the plan's are."""
+        if grads is None:
+            return
+        grads = list(grads)
+        if len(grads) != self.nparams:
+            raise ValueError(f"{len(grads)} gradients, the plan was made for {self.nparams}")
+        for p, (g, want) in enumerate(zip(grads, self._what)):
+            if (not isinstance(g, torch.Tensor) or not g.is_contiguous()
+                    or (g.data_ptr(), g.numel(), g.dtype) != want):
+                raise ValueError(f"grads[{p}] is not the tensor that the plan was made for: keep "
+                                 "the gradients (zero_grad(set_to_none=False)), or make a new "
+                                 "plan")
+
+    def norm(self, grads: Sequence[torch.Tensor] | None = None) -> torch.Tensor:
         """Enqueue the norm alone; nothing is written to the gradients."""
+        self._same(grads)
         self._list.norm(self._kind, None, self._norm, self.ws, 1)
         return self._norm
 
-    def total(self) -> torch.Tensor:
+    def total(self, grads: Sequence[torch.Tensor] | None = None) -> torch.Tensor:
         """Enqueue this rank's part of a norm over ranks (see grad_total)."""
+        self._same(grads)
         self._list.norm(self._kind, self._total, None, self.ws, 1)
         return self._total
 
-    def run(self, max_norm: float, total: torch.Tensor | None = None) -> torch.Tensor:
-        """Enqueue the clip; returns the norm before it without syncing."""
+    def run(self, max_norm: float, total: torch.Tensor | None = None,
+            grads: Sequence[torch.Tensor] | None = None) -> torch.Tensor:
+        """Enqueue the clip; returns the norm before it without syncing.  grads:
+        this step's, which must be the plan's."""
+        self._same(grads)
         self._list.clip(self._kind, _given_total(total, self.device), _max_norm(max_norm),
                         self._norm, self.ws, 1)
         return self._norm
