@@ -608,7 +608,7 @@ delta_status grad_norm_many(int32_t nparams, const void *const *grad_ptrs, const
 
 /*
  * grad_clip_many -- out = g * min(1, max_norm / (norm + 1e-6)) for every
- * tensor of a list, rounded once to its type.
+ * tensor of a list, the factor held in fp32, rounded once to its type.
  *  out_ptrs            (host) device pointers of the results, or null: in
  *                      place.  In place, a factor of 1 writes nothing.  No
  *                      tensor that is written may overlap another one

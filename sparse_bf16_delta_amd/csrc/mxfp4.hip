@@ -23,7 +23,11 @@
 // (310 tensors) takes 242-249 us, the way back 253-263: 1.51 GB each, moved
 // once as the counters show, at 6.0-6.2 and 5.8-6.0 TB/s, where bare streams
 // of the same bytes took 223 and 236 us.  One 1024 x 1024 tensor takes 2.9-3.1
-// us each way, which is a launch.  A delta of 7.2M entries (1.18 %) into 607M
+// us each way, which is a launch.  fp16 goes as bf16 does; fp32 quantises at 5.2
+// TB/s and comes back at 2.5 (36 tensors of 4096 x 4096, 531 and 1077 us; bf16
+// 247 and 284).  Rows that are no multiple of 32, bf16: 36 tensors of 4096 x 4097
+// 294 us and 323 back, 5.2 and 4.7 TB/s, without the next loads in flight and with
+// a division for every block.  A delta of 7.2M entries (1.18 %) into 607M
 // values takes 382-408 us: 0.77 GB read and 0.58 GB written at 3.4 TB/s, because
 // single blocks of 64 bytes are read and written back; without the stores of
 // the codes it took 312 us, without those of the snapshot 283.  The same delta

@@ -566,13 +566,31 @@ constexpr TileShape kTiles[] = {
     {256, 256, 8.5, 0.0, 1}, {128, 128, 2.9, 1.2, 2}, {64, 64, 1.0, 0.9, 4}};
 constexpr int kCus = 256;
 
-// Up to 32 rows of x, as long as reading them again for every 16 rows of w
-// stays small.  Measured against 64 x 64 tiles, us: 1 x 11008 x 4096 8.6 / 11.0,
-// 16 x 4096 x 11008 10.0 / 12.0, 16 x 32768 x 4096 23.6 / 15.4, 32 x 4096 x 4096
-// 8.0 / 10.1, 32 x 11008 x 4096 14.7 / 9.9, 45 x 4096 x 11008 15.2 / 13.9.
+// Up to 32 rows of x, as long as w has few rows: every 16 of them are a
+// workgroup that reads x again and joins its waves' sums.  Measured against 64 x
+// 64 tiles, us: 1 x 11008 x 4096 8.6 / 11.0, 16 x 4096 x 11008 10.0 / 12.0, 16 x
+// 32768 x 4096 23.6 / 15.4, 32 x 4096 x 4096 8.0 / 10.1, 32 x 11008 x 4096 14.7 /
+// 9.9, 45 x 4096 x 11008 15.2 / 13.9.  A single row is faster by tiles too where w
+// has many.  By rows / by tiles, x in MXFP4, and in bf16 and quantised in the call:
+//    1 x 16384 x 4096     9.5 / 11.3     9.6 / 14.1
+//   16 x 16384 x 4096    12.0 / 11.2    15.1 / 14.2
+//    1 x 28672 x 8192    29.8 / 23.2    35.6 / 25.9
+//    1 x 32000 x 4096    16.3 / 12.4    15.6 / 15.4
+//    4 x 32000 x 4096    17.5 / 12.5    22.3 / 15.4
+//    1 x 53248 x 16384   87.4 / 84.8    96.8 / 88.6
+//    1 x 128256 x 4096   55.0 / 46.7    55.7 / 50.1
+//    4 x 128256 x 4096   58.8 / 47.0    81.7 / 50.1
 bool by_rows(int64_t m, int64_t n) { return m <= 32 && (m + 15) / 16 * n <= 16384; }
 
-// Whether mxfp4_linear quantises x within mx_rows_kernel.
+// Whether mxfp4_linear quantises x within mx_rows_kernel: every workgroup does it
+// for itself, a launch in front of them once for all.  Measured within / in front,
+// us (m x n x k): up to kLdsX values 1 x 11008 x 4096 7.0 / 9.3, 4 x 4096 x 4096 5.7
+// / 7.0, 4 x 11008 x 4096 10.0 / 10.0, 1 x 4096 x 11008 7.6 / 9.3, 2 x 8192 x 8192
+// 10.8 / 11.5, 2 x 1024 x 8192 6.9 / 8.3, 8 x 16384 x 1024 9.7 / 10.4, and against
+// the rule 16 x 16384 x 1024 11.7 / 10.7; above it 4 x 4096 x 11008 11.1 / 9.7, 8 x
+// 4096 x 4096 7.2 / 7.3, 8 x 11008 x 4096 13.5 / 10.8, 4 x 8192 x 8192 13.2 / 12.3,
+// 8 x 1024 x 8192 11.4 / 9.0, 16 x 4096 x 4096 10.5 / 7.7, and against the rule 2 x
+// 4096 x 11008 8.5 / 9.4.
 constexpr int64_t kLdsX = 16384;  // values
 bool quantize_inside(int64_t m, int64_t n, int64_t k) {
   return m <= 16 && by_rows(m, n) && m * k <= kLdsX;
