@@ -20,7 +20,7 @@
 //
 // What bounds them: memory.  The norm of a 7B-shaped list (291 tensors, 13.48
 // GB of bf16, read once as the counters show) takes 1912-1924 us, 7.0 TB/s,
-// where reading two arrays without any arithmetic reaches 6.8-7.2; that of a
+// where reading two arrays without any arithmetic reaches 6.8-7.3; that of a
 // 0.6B-shaped one (310 tensors, 1.19 GB) 176-181 us, 6.7 TB/s, and its clip 398-405
 // us for 2.38 GB, 5.9 TB/s, where a bare stream that scales them took 370.  One
 // 1M tensor takes 3.0 + 4.0 us, two launches.  (Clipping from the list's end,
